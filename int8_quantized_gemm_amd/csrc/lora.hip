@@ -592,8 +592,8 @@ bool lora_direct(int64_t M, int64_t N, int R) {
   return M <= 256 || ((M + 15) / 16) * ((N + 255) / 256) * ((R + 31) / 32) <= 400;
 }
 
-// K ranges of the shrinking product: enough workgroups for the chip, at least
-// 256 K elements per range
+// K ranges of the shrinking product (M >= 1): enough workgroups for the chip, at
+// least 256 K elements per range
 int lora_splits(int64_t M, int64_t K) {
   const int rows = M <= kSlotRows ? 16 : 64;
   const int64_t tiles = (M + rows - 1) / rows;
@@ -677,6 +677,7 @@ hipError_t launch_lora_t(const LoraParams& p, hipStream_t st) {
 
 // partial sums, then (more than 256 rows) the two terms and the exponents
 size_t lora_part_bytes(int64_t M, int64_t K, int R) {
+  if (M == 0) return 0;
   size_t n = round16(lora_sum_bytes(M, K, R));
   if (M > 256) n += 2 * lora_term_bytes(M, R) + (size_t)M * 4;
   return n;
