@@ -631,7 +631,7 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     """Row stride of a 2-D tensor with unit column stride (its width for the
     shapes whose strides torch leaves arbitrary)."""
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if rows and cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     ld = t.stride(0) if rows > 1 else cols
     _need(ld >= cols, f"{name} rows overlap")

@@ -5,6 +5,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 LIB = os.path.join(ROOT, "int8_quantized_gemm_amd", "libq8gemm.so")
@@ -20,3 +21,21 @@ def test_size_queries_without_rows():
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == ["0"] * 7
+
+
+@pytest.fixture(scope="module")
+def q8():
+    import int8_quantized_gemm_amd as m
+    return m
+
+
+def test_empty_batches_of_any_strides(q8):
+    """torch calls a tensor without elements contiguous whatever its strides."""
+    w, a, b = torch.zeros(12, 16).bfloat16(), torch.zeros(3, 8, 16).bfloat16(), torch.zeros(3, 20, 8).bfloat16()
+    ids = torch.zeros(0, dtype=torch.int32)
+    for x in (torch.empty_strided((0, 16), (0, 0), dtype=torch.bfloat16), torch.zeros(16, 4).bfloat16().t()[:0]):
+        assert x.is_contiguous()
+        for call in (lambda: q8.gated_mm(x, w), lambda: q8.lora_mm(x, a, b, ids),
+                     lambda: q8.lora_mm(x, a, b, ids, base=torch.empty_strided((0, 20), (1, 7), dtype=torch.bfloat16))):
+            with pytest.raises(ValueError, match="on the GPU"):
+                call()
