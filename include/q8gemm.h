@@ -426,12 +426,16 @@ int gated_mm(const void* x, int64_t ld_x, const void* W, const void* delta, void
  *
  * dG and dU are evaluated in float32 and rounded once to dtype, in which form
  * the two products take them; the products are summed in float32 and rounded
- * once. dx, dW and d_gate_up ([M, 2I], the gradient of delta) are outputs;
- * any of them may be NULL, and none may overlap an input or another. With
- * M == 0, dW is all zeros.
+ * once. Q8_F16: a power of two common to all of [dG | dU] brings the largest
+ * finite value into [2^14, 2^15) for that rounding and is put back into the
+ * sums, so dx and dW are finite wherever they fit f16, and values down to 2^-29
+ * of the largest keep f16's precision. dx, dW and d_gate_up ([M, 2I], the
+ * gradient of delta, of dtype) are outputs; any of them may be NULL, and none
+ * may overlap an input or another. With M == 0, dW is all zeros.
  * workspace: gated_mm_backward_workspace_size bytes for the current device,
- * 16-byte aligned (the rounded [dG | dU], and float32 sums of a product's
- * ranges where it has few tiles); its contents need no initialisation.
+ * 16-byte aligned (the rounded [dG | dU], its largest values, and float32 sums
+ * of a product's ranges where it has few tiles); its contents need no
+ * initialisation.
  */
 size_t gated_mm_backward_workspace_size(int64_t M, int64_t I, int64_t K);
 int gated_mm_backward(const void* dh, const void* x, int64_t ld_x, const void* W, const void* gate_up,

@@ -703,7 +703,8 @@ def gated_mm_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
     ``grad_gate_up`` [M, 2I], when given, receives the gradient of the
     pre-activations, which is also that of ``delta``. The gradients of the
     pre-activations are rounded once to the operands' type before the two
-    products, which are summed in float32. No output may overlap an input or
+    products, which are summed in float32 (float16: after a common power of two is
+    taken out of them, so neither large nor small ones are lost). No output may overlap an input or
     another output.
     """
     act = _act(activation)

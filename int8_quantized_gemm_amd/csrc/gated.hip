@@ -17,7 +17,7 @@
 //             they are very few (tile16_sum adds the ranges' sums); tile16s_both
 //             dx and dW in one launch.
 // gated_stream  a few rows: W streamed once into MFMA registers.
-// gated_grad  dG and dU from dh, G and U (elementwise).
+// gated_grad  dG and dU from dh, G and U (elementwise); f16: gated_grad_max first.
 // FP8: gated8 (tiles of 256 x 256), gated8s and gated8_sum (few tiles, and K
 // blocks of 32), gated8_stream (a few rows), gated_quant (codes of float32 h).
 #include <type_traits>
@@ -49,7 +49,15 @@ struct T16Params {
   int pair;          // output (and delta / gate_up) rows 4-byte aligned, their widths even
   int S;             // tile16s: ranges of the contraction (for the host: 1 asks for one range)
   float* part;       // their sums [S][M][N, or 2N when gated], or null for S = 1
+  const int32_t* exp;  // f16 gradients: the power of two taken out of A
 };
+
+// A sum of an f16 gradient with the power of two put back.
+template <bool BF>
+__device__ __forceinline__ float2 put_back(float2 v, int e) {
+  if constexpr (BF) return v;
+  else return float2{__builtin_ldexpf(v.x, e), __builtin_ldexpf(v.y, e)};
+}
 
 // Stage layout of an operand read across rows (contraction index the row):
 // [64 contraction rows][ROWS columns], 16-byte chunk c of row k at position
@@ -348,6 +356,7 @@ __device__ __forceinline__ void tile16_body(const T16Params& p, int64_t m0, int6
   const int64_t nw = n0 + wn * TN;
   if constexpr (!GATED) {
     uint16_t* D = static_cast<uint16_t*>(p.D);
+    const int e = BF ? 0 : *p.exp;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -362,7 +371,7 @@ __device__ __forceinline__ void tile16_body(const T16Params& p, int64_t m0, int6
             // even lanes and block 1's to the odd ones
             const float2 o = TRB ? pair_lanes(x, y, odd) : float2{x, y};
             const int64_t n = nw + v * HN + (TRB ? (odd ? 15 + r16 : r16) : 2 * r16);
-            if (m < M) store2<BF>(D + m * p.ldd + n, o, n, N, pair);
+            if (m < M) store2<BF>(D + m * p.ldd + n, put_back<BF>(o, e), n, N, pair);
           }
         }
   } else {
@@ -586,6 +595,8 @@ __device__ __forceinline__ void tile16s_body(const T16Params& p, int64_t block, 
     return;
   }
   uint32_t dg[FM][2], du[FM][2];  // loaded ahead of the first store, which a wait for one would include
+  int e = 0;
+  if constexpr (!GATED && !BF) e = *p.exp;
   if constexpr (GATED) {
     if (p.delta) {
 #pragma unroll
@@ -622,7 +633,7 @@ __device__ __forceinline__ void tile16s_body(const T16Params& p, int64_t block, 
         const float x = acc[i][0][r], y = acc[i][1][r];
         const float2 o = TRB ? pair_lanes(x, y, odd) : float2{x, y};
         const int64_t n = n0 + wn * 32 + (TRB ? (odd ? 15 + r16 : r16) : 2 * r16);
-        if (m < M) store2<BF>(static_cast<uint16_t*>(p.D) + m * p.ldd + n, o, n, N, pair);
+        if (m < M) store2<BF>(static_cast<uint16_t*>(p.D) + m * p.ldd + n, put_back<BF>(o, e), n, N, pair);
       }
     }
 }
@@ -686,7 +697,7 @@ __global__ __launch_bounds__(256) void tile16_sum(T16Params p) {
     }
     gated_out<BF, ACT>(p, m, n, x, y, pair);
   } else {
-    store2<BF>(static_cast<uint16_t*>(p.D) + m * p.ldd + n, x, n, N, pair);
+    store2<BF>(static_cast<uint16_t*>(p.D) + m * p.ldd + n, put_back<BF>(x, BF ? 0 : *p.exp), n, N, pair);
   }
 }
 
@@ -1555,61 +1566,139 @@ __global__ __launch_bounds__(256) void gated_quant(T8Params P) {
 // ------------------------------------------------------------------------------
 // dgu [M, ld] = [dG | dU | 0]: rounded once to the operands' type, as the
 // matrix cores take it (one 16-bit rounding per product term; the sums stay in
-// float32). Columns 2I .. ld are zeros, so dx's contraction runs over whole
-// slabs. out: an optional second copy [M, 2I] without padding. Bound by memory:
-// 10 M I bytes (4096 x 2x7168: 294 MB). VEC: eight columns per thread (I a multiple of
-// 8, 16-byte aligned rows), else one.
+// float32). f16: a power of two is taken out of all of them first, so that the
+// largest finite one lies in [2^14, 2^15) (a value above f16's largest would make
+// a whole row of dx and of dW infinite, and gradients of 1e-6 keep four bits as
+// they are); gated_grad_max finds it, the products put it back. Columns 2I .. ld
+// are zeros, so dx's contraction runs over whole slabs. out: an optional second
+// copy [M, 2I] without padding, as it is. Bound by memory:
+// 10 M I bytes (4096 x 2x7168: 294 MB, 47 us); gated_grad_max reads 6 M I more
+// (176 MB, 44 us; 1003 x 2x1021: 4.4 us). VEC: eight columns per thread (I a
+// multiple of 8, 16-byte aligned rows), else one.
+template <bool BF, int ACT, bool VEC>
+struct GradLoad {
+  static constexpr int V = VEC ? 8 : 1;
+  uint32_t d[VEC ? 4 : 1], g[VEC ? 4 : 1], u[VEC ? 4 : 1];
+  // columns n .. n + V - 1 of row m
+  __device__ __forceinline__ GradLoad(const uint16_t* dh, const uint16_t* gu, int64_t m, int64_t n, int64_t I) {
+    const uint16_t* const pd = dh + m * I + n;
+    const uint16_t* const pg = gu + m * 2 * I + n;
+    if constexpr (VEC) {
+      const uint4 dq = *reinterpret_cast<const uint4*>(pd), gq = *reinterpret_cast<const uint4*>(pg),
+                  uq = *reinterpret_cast<const uint4*>(pg + I);
+      d[0] = dq.x, d[1] = dq.y, d[2] = dq.z, d[3] = dq.w;
+      g[0] = gq.x, g[1] = gq.y, g[2] = gq.z, g[3] = gq.w;
+      u[0] = uq.x, u[1] = uq.y, u[2] = uq.z, u[3] = uq.w;
+    } else {
+      d[0] = pd[0], g[0] = pg[0], u[0] = pg[I];
+    }
+  }
+  // dG and dU of column i
+  __device__ __forceinline__ float2 grad(int i) const {
+    auto at = [&](const uint32_t (&w)[VEC ? 4 : 1]) {
+      return i % 2 ? hi_f32<BF>(w[i / 2]) : lo_f32<BF>(w[i / 2]);
+    };
+    float a;
+    const float da = act_grad_f32<ACT>(at(g), a), dv = at(d);
+    return float2{dv * at(u) * da, dv * a};
+  }
+};
+
+// f16: the largest finite |dG| and |dU| of each workgroup's columns.
+// Indices in 32 bits: M ld stays below 2^31.
+constexpr int kMaxima = 512, kMaxThreads = 1024;
+
+template <int ACT, bool VEC>
+__global__ __launch_bounds__(kMaxThreads) void gated_grad_max(const uint16_t* __restrict__ dh,
+                                                              const uint16_t* __restrict__ gu, float* __restrict__ maxima,
+                                                              int64_t M, int64_t I) {
+  __shared__ float red[kMaxThreads / 64];
+  typedef GradLoad<false, ACT, VEC> Load;
+  const uint32_t per = (uint32_t)(I / Load::V), total = (uint32_t)M * per;
+  float top = 0.0f;
+  for (uint32_t i = blockIdx.x * kMaxThreads + threadIdx.x; i < total; i += gridDim.x * kMaxThreads) {
+    const uint32_t m = i / per, n = (i - m * per) * Load::V;
+    const Load q(dh, gu, m, n, I);
+#pragma unroll
+    for (int c = 0; c < Load::V; ++c) {
+      const float2 v = q.grad(c);
+      const float x = __builtin_fabsf(v.x), y = __builtin_fabsf(v.y);
+      // a comparison with NaN is false
+      if (x < __builtin_inff()) top = __builtin_fmaxf(top, x);
+      if (y < __builtin_inff()) top = __builtin_fmaxf(top, y);
+    }
+  }
+  top = wave_max_xor(top, 64);
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = top;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  top = wave_max_xor(threadIdx.x < kMaxThreads / 64 ? red[threadIdx.x] : 0.0f, 64);
+  if (threadIdx.x == 0) maxima[blockIdx.x] = top;
+}
+
+// maxima: n_max <= 512 of them (0: nothing is taken out); exp: the power of two
+// that the products put back.
 template <bool BF, int ACT, bool VEC>
 __global__ __launch_bounds__(256) void gated_grad(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu,
                                                   uint16_t* __restrict__ dgu, int64_t ld, uint16_t* __restrict__ out,
-                                                  int64_t M, int64_t I) {
-  constexpr int V = VEC ? 8 : 1;
+                                                  int64_t M, int64_t I, const float* __restrict__ maxima, int n_max,
+                                                  int32_t* __restrict__ exp) {
+  typedef GradLoad<BF, ACT, VEC> Load;
+  constexpr int V = Load::V;
+  int e = 0;
+  if constexpr (!BF) {
+    static_assert(kMaxima <= 512, "two maxima per thread");
+    __shared__ float red[4];
+    const int i = threadIdx.x, j = i + 256;
+    const float top = wave_max_xor(__builtin_fmaxf(i < n_max ? maxima[i] : 0.0f, j < n_max ? maxima[j] : 0.0f), 64);
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = top;
+    __syncthreads();
+    const float t = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
+    e = t > 0.0f ? __builtin_amdgcn_frexp_expf(t) - 15 : 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *exp = e;
+  }
+  auto rounded = [&](float a, float b) {
+    if constexpr (BF) return pack2<BF>(a, b);
+    else return pack2<BF>(__builtin_ldexpf(a, -e), __builtin_ldexpf(b, -e));
+  };
   // threads of a row: its columns, then the padding
-  const int64_t per = (ld - I) / V;
-  const int64_t total = M * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / per, n = (i - m * per) * V;
+  const uint32_t per = (uint32_t)((ld - I) / V), total = (uint32_t)M * per;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    const int64_t m = i / per, n = (i - (uint32_t)m * per) * V;
     if constexpr (VEC) {
       if (n >= I) {
         *reinterpret_cast<uint4*>(dgu + m * ld + I + n) = uint4{0, 0, 0, 0};
         continue;
       }
-      const uint4 dq = *reinterpret_cast<const uint4*>(dh + m * I + n);
-      const uint4 gq = *reinterpret_cast<const uint4*>(gu + m * 2 * I + n);
-      const uint4 uq = *reinterpret_cast<const uint4*>(gu + m * 2 * I + I + n);
-      const uint32_t dw[4] = {dq.x, dq.y, dq.z, dq.w}, gw[4] = {gq.x, gq.y, gq.z, gq.w}, uw[4] = {uq.x, uq.y, uq.z, uq.w};
-      uint32_t og[4], ou[4];
+      const Load q(dh, gu, m, n, I);
+      uint32_t og[4], ou[4], wg[4], wu[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float a0, a1;
-        const float d0 = lo_f32<BF>(dw[c]), d1 = hi_f32<BF>(dw[c]);
-        const float b0 = act_grad_f32<ACT>(lo_f32<BF>(gw[c]), a0), b1 = act_grad_f32<ACT>(hi_f32<BF>(gw[c]), a1);
-        og[c] = pack2<BF>(d0 * lo_f32<BF>(uw[c]) * b0, d1 * hi_f32<BF>(uw[c]) * b1);
-        ou[c] = pack2<BF>(d0 * a0, d1 * a1);
+        const float2 a = q.grad(2 * c), b = q.grad(2 * c + 1);
+        og[c] = rounded(a.x, b.x);
+        ou[c] = rounded(a.y, b.y);
+        wg[c] = pack2<BF>(a.x, b.x);
+        wu[c] = pack2<BF>(a.y, b.y);
       }
-      const uint4 vg = {og[0], og[1], og[2], og[3]}, vu = {ou[0], ou[1], ou[2], ou[3]};
-      *reinterpret_cast<uint4*>(dgu + m * ld + n) = vg;
-      *reinterpret_cast<uint4*>(dgu + m * ld + I + n) = vu;
+      *reinterpret_cast<uint4*>(dgu + m * ld + n) = uint4{og[0], og[1], og[2], og[3]};
+      *reinterpret_cast<uint4*>(dgu + m * ld + I + n) = uint4{ou[0], ou[1], ou[2], ou[3]};
       if (out) {
-        *reinterpret_cast<uint4*>(out + m * 2 * I + n) = vg;
-        *reinterpret_cast<uint4*>(out + m * 2 * I + I + n) = vu;
+        *reinterpret_cast<uint4*>(out + m * 2 * I + n) = uint4{wg[0], wg[1], wg[2], wg[3]};
+        *reinterpret_cast<uint4*>(out + m * 2 * I + I + n) = uint4{wu[0], wu[1], wu[2], wu[3]};
       }
     } else {
       if (n >= I) {
         dgu[m * ld + I + n] = 0;
         continue;
       }
-      const float d = out_bits_to_f32<BF>(dh[m * I + n]);
-      const float G = out_bits_to_f32<BF>(gu[m * 2 * I + n]);
-      const float U = out_bits_to_f32<BF>(gu[m * 2 * I + I + n]);
-      float a;
-      const float da = act_grad_f32<ACT>(G, a);
-      const uint32_t o = pack2<BF>(d * U * da, d * a);
+      const float2 a = Load(dh, gu, m, n, I).grad(0);
+      const uint32_t o = rounded(a.x, a.y);
       dgu[m * ld + n] = (uint16_t)o;
       dgu[m * ld + I + n] = (uint16_t)(o >> 16);
       if (out) {
-        out[m * 2 * I + n] = (uint16_t)o;
-        out[m * 2 * I + I + n] = (uint16_t)(o >> 16);
+        const uint32_t w = pack2<BF>(a.x, a.y);
+        out[m * 2 * I + n] = (uint16_t)w;
+        out[m * 2 * I + I + n] = (uint16_t)(w >> 16);
       }
     }
   }
@@ -1749,18 +1838,30 @@ hipError_t launch_gated_act(const GatedArgs& a, hipStream_t st) {
   return launch_tile16<false, false, true, ACT>(p, bf, static_cast<float*>(a.workspace), st);
 }
 
+// dgu, and the power of two that the f16 products put back, in exp (maxima: scratch)
 template <int ACT>
-void launch_grad_act(const GatedGradArgs& a, uint16_t* dgu, int64_t ld, uint16_t* out, hipStream_t st) {
+hipError_t launch_grad_act(const GatedGradArgs& a, uint16_t* dgu, int64_t ld, uint16_t* out, float* maxima, int32_t* exp,
+                           hipStream_t st) {
   const bool vec = a.I % 8 == 0 && ((uintptr_t)a.dh | (uintptr_t)a.gate_up | (uintptr_t)out) % 16 == 0;
-  const int64_t total = a.M * (ld - a.I) / (vec ? 8 : 1);
-  const int64_t blocks = (total + 255) / 256;
-  const dim3 gr((unsigned)(blocks < 65536 ? blocks : 65536)), bl(256);
   const auto* dh = static_cast<const uint16_t*>(a.dh);
   const auto* gu = static_cast<const uint16_t*>(a.gate_up);
   const bool bf = a.dtype == Q8_BF16;
+  int n_max = 0;
+  if (!bf && (a.dx || a.dW)) {
+    const int64_t blocks = (a.M * (a.I / (vec ? 8 : 1)) + kMaxThreads - 1) / kMaxThreads;
+    n_max = blocks < kMaxima ? (int)blocks : kMaxima;
+    hipLaunchKernelGGL((vec ? gated_grad_max<ACT, true> : gated_grad_max<ACT, false>), dim3(n_max), dim3(kMaxThreads), 0,
+                       st, dh, gu, maxima, a.M, a.I);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int64_t total = a.M * (ld - a.I) / (vec ? 8 : 1);
+  const int64_t blocks = (total + 255) / 256;
+  const dim3 gr((unsigned)(blocks < 65536 ? blocks : 65536)), bl(256);
   const auto kern = vec ? (bf ? gated_grad<true, ACT, true> : gated_grad<false, ACT, true>)
                         : (bf ? gated_grad<true, ACT, false> : gated_grad<false, ACT, false>);
-  hipLaunchKernelGGL(kern, gr, bl, 0, st, dh, gu, dgu, ld, out, a.M, a.I);
+  hipLaunchKernelGGL(kern, gr, bl, 0, st, dh, gu, dgu, ld, out, a.M, a.I, maxima, n_max, exp);
+  return hipGetLastError();
 }
 
 int64_t grad_ld(int64_t I) { return (2 * I + 63) / 64 * 64; }
@@ -1799,12 +1900,14 @@ static bool one_launch(const T16Params& x, const T16Params& w) {
   return t < apart;
 }
 
-// the padded gradients of the pre-activations, then the ranges' sums of dx or dW
+// the padded gradients of the pre-activations, the maxima and the power of two
+// (f16), then the ranges' sums of dx or dW
 static size_t dgu_bytes_of(int64_t M, int64_t I) { return (size_t)M * (size_t)grad_ld(I) * 2; }
+constexpr size_t kMaximaBytes = kMaxima * sizeof(float) + 16;
 size_t gated_grad_bytes(int64_t M, int64_t I, int64_t K) {
   if (M == 0) return 0;
   const size_t x = tile16_part_bytes(M, K, grad_ld(I), false), w = tile16_part_bytes(2 * I, K, M, false);
-  return dgu_bytes_of(M, I) + (x > w ? x : w);
+  return dgu_bytes_of(M, I) + kMaximaBytes + (x > w ? x : w);
 }
 
 hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t st) {
@@ -1816,11 +1919,12 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t st) {
   const int64_t ld = grad_ld(a.I);
   uint16_t* dgu = static_cast<uint16_t*>(a.workspace);
   uint16_t* out = static_cast<uint16_t*>(a.d_gate_up);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + dgu_bytes_of(a.M, a.I));
-  if (a.act == kSilu) launch_grad_act<kSilu>(a, dgu, ld, out, st);
-  else if (a.act == kGelu) launch_grad_act<kGelu>(a, dgu, ld, out, st);
-  else launch_grad_act<kGeluTanh>(a, dgu, ld, out, st);
-  hipError_t e = hipGetLastError();
+  float* maxima = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + dgu_bytes_of(a.M, a.I));
+  int32_t* exp = reinterpret_cast<int32_t*>(maxima + kMaxima);
+  float* part = maxima + kMaximaBytes / sizeof(float);
+  hipError_t e = a.act == kSilu   ? launch_grad_act<kSilu>(a, dgu, ld, out, maxima, exp, st)
+                 : a.act == kGelu ? launch_grad_act<kGelu>(a, dgu, ld, out, maxima, exp, st)
+                                  : launch_grad_act<kGeluTanh>(a, dgu, ld, out, maxima, exp, st);
   if (e != hipSuccess) return e;
   const uint32_t dgu_bytes = (uint32_t)(a.M * ld * 2);
   T16Params x{}, w{};
@@ -1834,6 +1938,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t st) {
   w.M = 2 * a.I; w.N = a.K; w.C = a.M; w.a_cols = ld;
   w.D = a.dW; w.ldd = a.K;
   w.pair = (uintptr_t)a.dW % 4 == 0;
+  x.exp = w.exp = exp;
   const bool one = one_launch(x, w);
   // a gradient comes out the same whether or not the other is asked for
   if (one) x.S = w.S = 1;

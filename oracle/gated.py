@@ -51,8 +51,10 @@ def gated(gu, err, name):
     return h, gu, eh, err
 
 
-def backward(dh, x, w, gu, name, dtype):
-    """dx, dW, [dG | dU] and bounds of their errors before the last rounding."""
+def backward(dh, x, w, gu, name, dtype, tiny=None):
+    """dx, dW, [dG | dU] and bounds of their errors before the last rounding.
+    tiny: half a step of the smallest values of the rounded [dG | dU] that the
+    products take (default: of the plain type)."""
     I = gu.shape[1] // 2
     g, u = gu[:, :I], gu[:, I:]
     a, da = act(g, name)
@@ -61,7 +63,7 @@ def backward(dh, x, w, gu, name, dtype):
     # rounding to the operands' type
     scale = np.concatenate([np.abs(dh * u) * (1 + np.abs(g)), np.abs(dh * g)], axis=1)
     ed = 32 * F32 * scale
-    er = ed + HALF_STEP[dtype] * np.abs(d) + TINY[dtype]
+    er = ed + HALF_STEP[dtype] * np.abs(d) + (TINY[dtype] if tiny is None else tiny)
     n, m = d.shape[1], d.shape[0]
     dx, dw = d @ w, d.T @ x
     ex = er @ np.abs(w) + (n + 2) * F32 * (np.abs(d) @ np.abs(w))

@@ -1,0 +1,77 @@
+"""gated_mm and gated_mm_backward at the edge of what they allow, and their
+kernels over many slabs, ranges and rounds, against the float64 oracle."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import gated as og
+from tests.gpu_util import DEV, q8
+from tests.test_gpu_gated import T, check, f64, make
+
+pytestmark = pytest.mark.gpu
+
+
+def gradients(M, K, I, name, dh_std, u_std, w_std, x_std, seed=0):
+    """f16 operands of a backward pass, the gradients and their bounds: float32
+    sums, and [dG | dU] rounded once to f16 with its largest value brought to
+    [2^14, 2^15), so that the smallest values are off by 2^-25 of 2^(e - 15), with
+    2^e the power of two above the largest (one more where the kernel's float32
+    value lies across a power of two)."""
+    x, w = make((M, K), "f16", [seed, 1], x_std), make((2 * I, K), "f16", [seed, 2], w_std)
+    gu, dh = make((M, 2 * I), "f16", [seed, 3], 1.5), make((M, I), "f16", [seed, 4], dh_std)
+    gu[:, I:] *= u_std
+    d = og.backward(f64(dh), np.zeros((M, 1)), np.zeros((2 * I, 1)), f64(gu), name, "f16")[0][2]
+    e = math.frexp(np.abs(d).max())[1] + 1
+    ref = og.backward(f64(dh), f64(x), f64(w), f64(gu), name, "f16", 2.0 ** (e - 15 - 25))
+    return (dh, x, w, gu), ref
+
+
+# one launch for both products; ranges of the contraction; large tiles; few rows
+SHAPES = [(200, 264, 130), (700, 136, 40), (140, 136, 1500), (2100, 2056, 131), (300, 2056, 1100), (20, 72, 45)]
+
+
+# the activations differ in the first kernels only
+@pytest.mark.parametrize("M,K,I,name", [(*s, "silu") for s in SHAPES] +
+                         [(*s, n) for s in SHAPES[:1] + SHAPES[5:] for n in ("gelu", "gelu_tanh")])
+def test_f16_gradients_of_small_values(M, K, I, name):
+    """Gradients of 1e-6, among f16's subnormals, whose sums with large operands are
+    ordinary numbers."""
+    args, ((wx, ww, _), (ex, ew, _)) = gradients(M, K, I, name, 1e-6, 1.0, 30 * K ** -0.5, 30.0)
+    dx, dw = q8().gated_mm_backward(*[t.to(DEV) for t in args], name)
+    check(dx, wx, ex, "f16", "dx")
+    check(dw, ww, ew, "f16", "dW")
+
+
+@pytest.mark.parametrize("M,K,I", SHAPES)
+def test_f16_gradients_above_the_largest_f16(M, K, I):
+    """Gradients of the pre-activations of up to 1e6 between small operands."""
+    args, ((wx, ww, wd), (ex, ew, ed)) = gradients(M, K, I, "silu", 300.0, 300.0, 2.0 ** -10, 2.0 ** -10)
+    assert np.abs(wd).max() > 2 * 65504
+    grad_gate_up = torch.empty((M, 2 * I), dtype=torch.float16, device=DEV)
+    dx, dw = q8().gated_mm_backward(*[t.to(DEV) for t in args], grad_gate_up=grad_gate_up)
+    check(dx, wx, ex, "f16", "dx")
+    check(dw, ww, ew, "f16", "dW")
+    # the gradient of the pre-activations itself is an f16 output
+    got, fits = f64(grad_gate_up), np.abs(wd) < 65000
+    assert not og.within(got[fits], wd[fits], ed[fits], "f16").any()
+    assert np.isinf(got[np.abs(wd) > 66000]).all()
+
+
+def test_f16_gradients_beside_a_row_that_is_not_finite():
+    M, K, I = 200, 264, 130
+    args, ((wx, _, _), (ex, _, _)) = gradients(M, K, I, "silu", 1e-6, 1.0, 30 * K ** -0.5, 30.0)
+    dh = args[0].clone()
+    dh[7, 3], dh[9, 5] = float("inf"), float("nan")
+    dx, _ = q8().gated_mm_backward(*[t.to(DEV) for t in (dh, *args[1:])])
+    keep = [i for i in range(M) if i not in (7, 9)]
+    check(dx[keep], wx[keep], ex[keep], "f16", "dx")
+    assert not torch.isfinite(dx[[7, 9]]).any()
+
+
+def test_f16_gradients_that_are_all_zero():
+    M, K, I = 70, 72, 40
+    args, _ = gradients(M, K, I, "silu", 1.0, 1.0, 1.0, 1.0)
+    dx, dw = q8().gated_mm_backward(*[t.to(DEV) for t in (torch.zeros_like(args[0]), *args[1:])])
+    assert (dx == 0).all() and (dw == 0).all()
