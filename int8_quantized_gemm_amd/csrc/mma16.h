@@ -96,11 +96,13 @@ __device__ __forceinline__ float act_grad_f32(float g, float& a) {
     a = g * phi;
     return __builtin_fmaf(g * 0.39894228040143267794f, exp_f32(-0.5f * g * g), phi);
   } else {
-    // s = sigmoid(2y): s' = 2 s (1 - s) y'
+    // s = sigmoid(2y): s' = 2 s (1 - s) y'; y' is kept finite, as s (1 - s) = 0
+    // where it would overflow
     const float y2 = 2.0f * kGeluC * __builtin_fmaf(kGeluA * g * g, g, g);
     const float s = sigmoid_f32(y2);
     a = g * s;
-    return __builtin_fmaf(a * (1.0f - s), 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluA * g, g, 1.0f), s);
+    const float dy = __builtin_fminf(__builtin_fmaf(3.0f * kGeluA * g, g, 1.0f), 1e38f);
+    return __builtin_fmaf(a * (1.0f - s), 2.0f * kGeluC * dy, s);
   }
 }
 

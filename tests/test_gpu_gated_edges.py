@@ -75,3 +75,25 @@ def test_f16_gradients_that_are_all_zero():
     args, _ = gradients(M, K, I, "silu", 1.0, 1.0, 1.0, 1.0)
     dx, dw = q8().gated_mm_backward(*[t.to(DEV) for t in (torch.zeros_like(args[0]), *args[1:])])
     assert (dx == 0).all() and (dw == 0).all()
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gradients_at_pre_activations_of_any_size(name, dtype):
+    """act and act' from the smallest to the largest finite pre-activations."""
+    top = float(torch.finfo(T[dtype]).max)
+    g = [10.0 ** e for e in range(-7, 39) if 10.0 ** e < top] + [0.0, 0.5, 2.0, 3.0, 5.5, 20.0, 85.0, top]
+    g = torch.tensor(sorted(g + [-v for v in g])).to(T[dtype])[None]
+    I, K = g.shape[1], 8
+    u, dh = torch.full_like(g, 0.75), torch.full_like(g, 0.5)
+    gu = torch.cat([g, u], 1)
+    d = torch.empty((1, 2 * I), dtype=T[dtype], device=DEV)
+    q8().gated_mm_backward(dh.to(DEV), torch.zeros((1, K), dtype=T[dtype], device=DEV),
+                           torch.zeros((2 * I, K), dtype=T[dtype], device=DEV), gu.to(DEV), name, need_x=False, need_w=False,
+                           grad_gate_up=d)
+    (_, _, want), (_, _, err) = og.backward(f64(dh), np.zeros((1, K)), np.zeros((2 * I, K)), f64(gu), name, dtype)
+    # the derivative's own error (oracle/gated.py: 32 half steps of 1 + |g|) is that of
+    # values near the bend; past it act' is 0 or 1 to float32
+    far = np.abs(np.concatenate([f64(g), f64(g)], 1)) > 200
+    err = np.where(far, 4 * og.F32 * np.abs(want), err)
+    check(d, want, err, dtype, name)
