@@ -261,10 +261,15 @@ __device__ __forceinline__ void split16(const float (&v)[8], i32x4& hi, i32x4& l
   }
 }
 
-// Power of two just above big (0 where big is 0 or not finite).
-__device__ __forceinline__ int row_exp(float big) {
-  return big > 0.0f && big < __builtin_inff() ? __builtin_amdgcn_frexp_expf(big) : 0;
+// The larger of big and |v| where v is finite: infinities and NaN stay what they
+// are in any scale, and the finite values beside them need theirs.
+__device__ __forceinline__ float larger_finite(float big, float v) {
+  const float a = __builtin_fabsf(v);
+  return a < __builtin_inff() ? __builtin_fmaxf(big, a) : big;
 }
+
+// Power of two just above big (0 where big is 0).
+__device__ __forceinline__ int row_exp(float big) { return big > 0.0f ? __builtin_amdgcn_frexp_expf(big) : 0; }
 
 // The expanding product has the rows' terms as operand 0 and B_a's rows (output
 // columns) as operand 1, column 4 r16 + j of a wave's 64 in MFMA j: lane (g, r16)
@@ -383,7 +388,7 @@ __global__ __launch_bounds__(256) void lora_expand(LoraParams p) {
         v[kt][4 + i] = x1[i] * sc;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) big = __builtin_fmaxf(big, __builtin_fabsf(v[kt][i]));
+      for (int i = 0; i < 8; ++i) big = larger_finite(big, v[kt][i]);
     }
     big = __builtin_fmaxf(big, __shfl_xor(big, 16, 64));
     big = __builtin_fmaxf(big, __shfl_xor(big, 32, 64));
@@ -456,7 +461,7 @@ __global__ __launch_bounds__(256) void lora_join(LoraParams p) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[i] = (i < 4 ? x0[i & 3] : x1[i & 3]) * sc;
-    big = __builtin_fmaxf(big, __builtin_fabsf(v[i]));
+    big = larger_finite(big, v[i]);
   }
 #pragma unroll
   for (int d = 1; d < 16; d <<= 1) big = __builtin_fmaxf(big, __shfl_xor(big, d, 64));

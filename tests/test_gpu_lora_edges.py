@@ -15,3 +15,18 @@ def test_no_rows():
     assert q8().lora_mm(x, a, b, it).shape == (0, 48)
     assert q8().lora_mm(x, a, b, it, torch.ones(2, device=DEV), base=base).shape == (0, 48)
     assert q8().lora_mm(x, a, b, it, base=base, out=base) is base
+
+
+@pytest.mark.parametrize("M", [3, 600, 1100])  # the last through lora_join
+def test_an_infinite_rank_beside_values_above_f16(M):
+    """One infinite term of x A^T leaves the others what they are: they lie above
+    f16's largest value and must not become infinities of the other sign."""
+    K, N, R = 64, 1700, 16
+    x = torch.full((M, K), 40.0, dtype=torch.float16)
+    a = torch.full((1, R, K), 40.0, dtype=torch.float16)
+    a[0, 5, 3] = float("inf")
+    b = torch.full((1, N, R), -1.0, dtype=torch.float16)
+    b[0, :, 5] = 1.0
+    ids = torch.zeros(M, dtype=torch.int32)
+    got = q8().lora_mm(*[t.to(DEV) for t in (x, a, b, ids)])
+    assert (got == float("inf")).all()
