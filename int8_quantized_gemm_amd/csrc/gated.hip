@@ -791,6 +791,13 @@ struct T8Params {
   int bf16, act;
 };
 
+// Wave-uniform offset of a slab's scales. The range check compares the lane's offset
+// with the buffer's size less the uniform one, which must not pass that size: a
+// buffer of a few scales is shorter than the slabs copied ahead of the last. (The
+// operands' sizes and slabs are multiples of 16 bytes, and kNowhere lies
+// sixteen below the end of the offsets.)
+__device__ __forceinline__ uint32_t scale_at(int64_t left, int off) { return left > 0 ? (uint32_t)off : 0u; }
+
 template <int KS, int BM, int WM, int NC>
 __global__ __launch_bounds__(512, 2) void gated8s(T8Params P) {
   constexpr int NW = 8, WN = NW / WM, BN = 32 * WN * NC, FM = BM / WM / 16;
@@ -852,12 +859,13 @@ __global__ __launch_bounds__(512, 2) void gated8s(T8Params P) {
     oa.issue(kt, left, l, w);
     ob.issue(kt, left, l + BM * 128, w);
     uint8_t* const ls = l + (BM + BN) * 128;
+    const uint32_t at = scale_at(left, kt * SB);
     if constexpr (KS == 128) {
-      b2l4(rs, left > 0 ? soff : kNowhere, kt * SB, ls + sq * 64 * SB);
-      b2l4(rw, left > 0 ? woff : kNowhere, kt * SB, ls + BM * SB);
+      b2l4(rs, left > 0 ? soff : kNowhere, at, ls + sq * 64 * SB);
+      b2l4(rw, left > 0 ? woff : kNowhere, at, ls + BM * SB);
     } else {
-      b2l16(rs, left > 0 ? soff : kNowhere, kt * SB, ls + sq * 64 * SB);
-      b2l16(rw, left > 0 ? woff : kNowhere, kt * SB, ls + BM * SB);
+      b2l16(rs, left > 0 ? soff : kNowhere, at, ls + sq * 64 * SB);
+      b2l16(rw, left > 0 ? woff : kNowhere, at, ls + BM * SB);
     }
   };
   auto step = [&](int kt, uint8_t* __restrict__ nl, const uint8_t* __restrict__ la) {
@@ -1141,12 +1149,13 @@ __device__ __forceinline__ void gated8_body(const T8Params& P, int64_t m0, int64
   auto left = [&](int k) { return p.C - (int64_t)k * 64; };
   auto issue_a0 = [&](int k, uint8_t* l) {
     oa[0].issue(k, left(k), l, w);
-    b2l4(rs, left(k) > 0 ? soff[0] : kNowhere, k * 4, l + 128 * 128 + w % 2 * 256);
-    b2l4(rw, left(k) > 0 ? woff : kNowhere, k * 4, l + 128 * 128 + 512);
+    const uint32_t at = scale_at(left(k), k * 4);
+    b2l4(rs, left(k) > 0 ? soff[0] : kNowhere, at, l + 128 * 128 + w % 2 * 256);
+    b2l4(rw, left(k) > 0 ? woff : kNowhere, at, l + 128 * 128 + 512);
   };
   auto issue_a1 = [&](int k, uint8_t* l) {
     oa[1].issue(k, left(k), l, w);
-    b2l4(rs, left(k) > 0 ? soff[1] : kNowhere, k * 4, l + 128 * 128 + w % 2 * 256);
+    b2l4(rs, left(k) > 0 ? soff[1] : kNowhere, scale_at(left(k), k * 4), l + 128 * 128 + w % 2 * 256);
   };
   constexpr int A0 = L + 2, A1 = L + 1, B = L;
   f32x4 acc[H][2][FM][FN];
