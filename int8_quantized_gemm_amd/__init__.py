@@ -610,6 +610,22 @@ def _act(name: str) -> int:
     return a
 
 
+def _scratch_size(dev: int, fn, *args) -> int:
+    """A workspace-size query answered for device ``dev`` (its compute units count),
+    memoised per device and shape."""
+    key = (fn.__name__, dev, args)
+    n = _ws_sizes.get(key)
+    if n is None:
+        if torch.cuda.current_device() == dev:
+            n = fn(*args)
+        else:
+            with torch.cuda.device(dev):
+                n = fn(*args)
+        if len(_ws_sizes) < 4096:
+            _ws_sizes[key] = n
+    return n
+
+
 def _own_scratch(dev: int, nbytes: int):
     """Workspace of one call, from torch's caching allocator: stream-ordered
     reuse, and under graph capture memory of the graph's own pool, so no two
@@ -685,7 +701,7 @@ def gated_mm(x: torch.Tensor, w: torch.Tensor, activation: str = "silu", *,
     dev = _dev(x, w, delta, gate_up, out)
     if out is None:
         out = torch.empty((M, I), dtype=dt, device=dev)
-    nbytes = _ws_size(_gated_ws, M, I, K)
+    nbytes = _scratch_size(dev, _gated_ws, M, I, K)
     ws = _own_scratch(dev, nbytes)
     _call(dev, _gated, x.data_ptr(), ldx, w.data_ptr(), _ptr(delta), _ptr(gate_up), out.data_ptr(), _DT[dt],
           act, M, I, K, _ptr(ws), nbytes)
@@ -724,7 +740,7 @@ def gated_mm_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
         grad_x = torch.empty((M, K), dtype=dt, device=dev)
     if need_w and grad_w is None:
         grad_w = torch.empty((2 * I, K), dtype=dt, device=dev)
-    nbytes = _ws_size(_gatedb_ws, M, I, K)
+    nbytes = _scratch_size(dev, _gatedb_ws, M, I, K)
     ws = _own_scratch(dev, nbytes)
     _call(dev, _gatedb, grad_out.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), gate_up.data_ptr(),
           _ptr(grad_x), _ptr(grad_w), _ptr(grad_gate_up), _DT[dt], act, M, I, K, _ptr(ws), nbytes)
@@ -787,7 +803,7 @@ def blockwise_scaled_gated_mm(mat_a: torch.Tensor, mat_b: torch.Tensor, scales_a
         out = torch.empty((M, I), dtype=out_dtype, device=dev)
     if quant and out_scales is None:
         out_scales = torch.empty((M, I // 128), dtype=torch.float32, device=dev)
-    nbytes = _ws_size(_bgated_ws, M, I, K, bn, bk, int(quant))
+    nbytes = _scratch_size(dev, _bgated_ws, M, I, K, bn, bk, int(quant))
     ws = _own_scratch(dev, nbytes)
     o = out.data_ptr()
     _call(dev, _bgated, mat_a.data_ptr(), scales_a.data_ptr(), mat_b.data_ptr(), scales_b.data_ptr(),
@@ -838,7 +854,7 @@ def lora_mm(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, adapter
     if out is None:
         out = torch.empty((M, N), dtype=dt, device=dev)
         ldo = N
-    nbytes = _ws_size(_lora_ws, M, K, R)
+    nbytes = _scratch_size(dev, _lora_ws, M, K, R)
     ws = _own_scratch(dev, nbytes)
     _call(dev, _lora, x.data_ptr(), ldx, lora_a.data_ptr(), lora_b.data_ptr(), adapter_ids.data_ptr(),
           _ptr(scaling), _ptr(base), ldb, out.data_ptr(), ldo, _DT[dt], M, N, K, R, L, _ptr(ws), nbytes)

@@ -39,3 +39,29 @@ def test_empty_batches_of_any_strides(q8):
                      lambda: q8.lora_mm(x, a, b, ids, base=torch.empty_strided((0, 20), (1, 7), dtype=torch.bfloat16))):
             with pytest.raises(ValueError, match="on the GPU"):
                 call()
+
+
+def test_sizes_are_asked_for_on_the_tensors_device(q8, monkeypatch):
+    """The workspace of a call depends on its device's compute units, whichever device
+    is current, and is remembered for each."""
+    now, asked = [0], []
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.d
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+
+    def sizes(M, I):
+        asked.append(now[0])
+        return 100 * (now[0] + 1) + M + I
+
+    monkeypatch.setattr(q8.torch.cuda, "device", Device)
+    monkeypatch.setattr(q8.torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(q8, "_ws_sizes", {})
+    assert [q8._scratch_size(d, sizes, 3, 4) for d in (0, 1, 0, 1)] == [107, 207, 107, 207]
+    assert asked == [0, 1] and now == [0]
