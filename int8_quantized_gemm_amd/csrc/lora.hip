@@ -641,9 +641,10 @@ hipError_t launch_expand_v(LoraParams p, hipStream_t st) {
     hipLaunchKernelGGL((lora_expand<KT, BF, VEC>), dim3((unsigned)tiles, ny, slots), dim3(256), 0, st, p);
   } else {
     // the fewest blocks per workgroup with which every workgroup is resident at
-    // once, three (two above rank 64) to a compute unit: 4096 x 7168, rank 64,
-    // eight blocks, 896 workgroups 41 us, ten, 728 34 us
-    const int64_t room = (KT <= 2 ? 768 : 512) / ny;
+    // once, three (two above rank 64) to a compute unit: 4096 x 7168, rank 64, 256
+    // units, eight blocks, 896 workgroups 41 us, ten, 728 34 us
+    const int cus = device_cus();
+    const int64_t room = (KT <= 2 ? 3 : 2) * (int64_t)(cus > 0 ? cus : 256) / ny;
     const int64_t nb = room < 1 ? 16 : (tiles + room - 1) / room;
     p.nb = nb > 16 ? 16 : (int)nb;
     const int64_t grid = (tiles + p.nb - 1) / p.nb * ny;
