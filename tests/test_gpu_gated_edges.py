@@ -8,7 +8,7 @@ import torch
 
 from oracle import gated as og
 from tests.gpu_util import DEV, q8
-from tests.test_gpu_gated import T, check, f64, make
+from tests.test_gpu_gated import T, back, check, f64, make
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,41 @@ def test_gradients_at_pre_activations_of_any_size(name, dtype):
     far = np.abs(np.concatenate([f64(g), f64(g)], 1)) > 200
     err = np.where(far, 4 * og.F32 * np.abs(want), err)
     check(d, want, err, dtype, name)
+
+
+# on 256 compute units: large tiles, whole (3 and 8 slabs) and all in halves (5), with
+# the last 32 of 288 in halves (7); a split contraction in tiles of 128 and of 64 rows
+@pytest.mark.parametrize("M,K,I", [(3850, 136, 1701), (3850, 456, 1700), (2100, 264, 1031), (4400, 392, 1930),
+                                   (100, 2568, 63), (300, 2568, 259), (20, 2568, 64)])
+@pytest.mark.parametrize("name,dtype", [("silu", "bf16"), ("gelu", "f16")])
+def test_forward_delta(M, K, I, name, dtype):
+    x, w = make((M, K), dtype, 1), make((2 * I, K), dtype, 2, K ** -0.5)
+    delta = make((M, 2 * I), dtype, 3, 2.0)
+    gate_up = torch.empty((M, 2 * I), dtype=T[dtype], device=DEV)
+    h = q8().gated_mm(x.to(DEV), w.to(DEV), name, delta=delta.to(DEV), gate_up=gate_up)
+    want, gu, eh, eg = og.forward(f64(x), f64(w), name, f64(delta))
+    check(h, want, eh, dtype, "h")
+    check(gate_up, gu, eg, dtype, "gate_up")
+
+
+def test_forward_rows_that_are_not_aligned():
+    """Outputs and delta two bytes past an aligned address, in every kernel."""
+    for M, K, I in ((3, 136, 66), (40, 136, 66), (100, 136, 66), (100, 2568, 66), (2100, 136, 1030)):
+        x, w, delta = make((M, K), "bf16", 1), make((2 * I, K), "bf16", 2, K ** -0.5), make((M, 2 * I), "bf16", 3)
+        gate_up = torch.empty((M, 2 * I), dtype=torch.bfloat16, device=DEV)
+        ref = q8().gated_mm(x.to(DEV), w.to(DEV), delta=delta.to(DEV), gate_up=gate_up)
+        off = lambda t: torch.cat([t.flatten()[:1], t.flatten(), t.flatten()[:1]])[1:-1].view(t.shape)  # noqa: E731
+        d, gu, out = off(delta.to(DEV)), off(torch.zeros_like(gate_up)), off(torch.zeros_like(ref))
+        assert d.data_ptr() % 4 == 2 and out.data_ptr() % 4 == 2
+        assert torch.equal(q8().gated_mm(x.to(DEV), w.to(DEV), delta=d, gate_up=gu, out=out), ref)
+        assert torch.equal(gu, gate_up)
+
+
+# dx, then dW, in large tiles over four slabs and more: whole, in halves, and the last
+# of 306 in halves; either in ranges of its contraction
+@pytest.mark.parametrize("M,K,I", [(3600, 3208, 131), (3600, 3208, 128), (4400, 4104, 100), (2100, 2056, 131),
+                                   (333, 3208, 1900), (300, 3208, 1901), (257, 4104, 2200), (300, 2056, 1100),
+                                   (100, 200, 1400), (300, 136, 1300), (2600, 200, 50), (2600, 264, 131)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_backward_long_contractions(M, K, I, dtype):
+    back(M, K, I, dtype, "silu")
