@@ -689,6 +689,12 @@ def gated_mm(x: torch.Tensor, w: torch.Tensor, activation: str = "silu", *,
     ``delta`` [M, 2I] is added before the activation (a low-rank adapter's part,
     ``lora_mm``); ``gate_up`` [M, 2I], when given, receives the
     pre-activations that ``gated_mm_backward`` takes. K must be a multiple of 8.
+    No output may overlap an input or another output.
+
+    Like every function here it leaves no autograd graph, also where ``x`` or
+    ``w`` require gradients: for training, call it in the ``forward`` of a
+    ``torch.autograd.Function`` that saves ``gate_up``, and
+    ``gated_mm_backward`` in its ``backward`` (``grad_out`` made contiguous).
     """
     act = _act(activation)
     dt, M, I, K, ldx = _check_gated(x, w)
@@ -712,8 +718,9 @@ def gated_mm_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
                       activation: str = "silu", *, need_x: bool = True, need_w: bool = True,
                       grad_x: torch.Tensor | None = None, grad_w: torch.Tensor | None = None,
                       grad_gate_up: torch.Tensor | None = None):
-    """Gradients ``(grad_x, grad_w)`` of ``gated_mm`` from ``grad_out`` [M, I] and
-    the pre-activations ``gate_up`` [M, 2I] that the forward call wrote.
+    """Gradients ``(grad_x, grad_w)`` of ``gated_mm`` from ``grad_out`` [M, I]
+    (contiguous) and the pre-activations ``gate_up`` [M, 2I] that the forward call
+    wrote.
 
     ``need_x`` / ``need_w`` False leaves that gradient out (None);
     ``grad_gate_up`` [M, 2I], when given, receives the gradient of the

@@ -135,3 +135,86 @@ def test_forward_rows_that_are_not_aligned():
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_backward_long_contractions(M, K, I, dtype):
     back(M, K, I, dtype, "silu")
+
+
+class GatedMM(torch.autograd.Function):
+    """gated_mm in a graph, as its documentation says a caller writes it."""
+
+    @staticmethod
+    def forward(ctx, x, w, activation):
+        gate_up = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
+        h = q8().gated_mm(x, w, activation, gate_up=gate_up)
+        ctx.save_for_backward(x, w, gate_up)
+        ctx.activation = activation
+        return h
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        x, w, gate_up = ctx.saved_tensors
+        gx, gw = q8().gated_mm_backward(grad_out.contiguous(), x, w, gate_up, ctx.activation,
+                                        need_x=ctx.needs_input_grad[0], need_w=ctx.needs_input_grad[1])
+        return gx, gw, None
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_autograd_function(dtype):
+    """Eager, with one gradient only, and captured while no eager graph of the leaves
+    lives; replayed with the program's own steps between."""
+    M, K, I = 150, 200, 90
+    x, w, c = make((M, K), dtype, 1).to(DEV), make((2 * I, K), dtype, 2, K ** -0.5).to(DEV), make((M, I), dtype, 3).to(DEV)
+    gate_up = torch.empty((M, 2 * I), dtype=T[dtype], device=DEV)
+    h = q8().gated_mm(x, w, "gelu_tanh", gate_up=gate_up)
+    ref = q8().gated_mm_backward(c, x, w, gate_up, "gelu_tanh")
+    xl, wl = x.clone().requires_grad_(True), w.clone().requires_grad_(True)
+    # the call itself leaves no graph
+    assert q8().gated_mm(xl, wl).requires_grad is False
+
+    def step():
+        y = GatedMM.apply(xl, wl, "gelu_tanh")
+        return y.detach(), *torch.autograd.grad(y, (xl, wl), c)
+
+    assert all(torch.equal(a, b) for a, b in zip(step(), (h, *ref)))
+    y = GatedMM.apply(xl, w, "gelu_tanh")
+    assert torch.equal(torch.autograd.grad(y, xl, c)[0], ref[0])
+    # a gradient without strides of its own
+    y = GatedMM.apply(xl, wl, "gelu_tanh")
+    one = torch.autograd.grad(y.float().sum(), wl)[0]
+    assert torch.equal(one, q8().gated_mm_backward(torch.ones_like(c), x, w, gate_up, "gelu_tanh")[1])
+    del y
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for k in range(3):
+        with torch.no_grad():
+            xl.copy_(x.roll(k, 0))
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
+        torch.cuda.synchronize()
+
+
+def test_two_streams_at_once():
+    """Backward passes of different sizes side by side: each call has its workspace."""
+    m = q8()
+    sets = []
+    for M, K, I, dtype in ((700, 136, 40, "f16"), (100, 200, 1400, "f16"), (300, 264, 130, "bf16")):
+        t = [make((M, I), dtype, 4), make((M, K), dtype, 1), make((2 * I, K), dtype, 2, K ** -0.5), make((M, 2 * I), dtype, 3)]
+        sets.append([v.to(DEV) for v in t])
+    ref = [m.gated_mm_backward(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                outs.append(m.gated_mm_backward(*s))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert all(torch.equal(a, b) for a, b in zip(o, ref[i % 3]))
