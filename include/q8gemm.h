@@ -406,8 +406,9 @@ typedef enum {
  * gate_up  [M, 2I] contiguous output: [G | U] rounded to dtype, as the backward
  *          pass takes it, or NULL
  * h        [M, I] contiguous output
- * K a multiple of 8; x and W 16-byte aligned. x and W must each stay below
- * 4 GiB less 256 rows. M == 0 is a no-op. I >= 1.
+ * Neither output may overlap an input or the other one. K a multiple of 8; x
+ * and W 16-byte aligned. x and W must each stay below 4 GiB less 256 rows.
+ * M == 0 is a no-op. I >= 1.
  * workspace: gated_mm_workspace_size bytes for the current device, 16-byte
  * aligned (float32 sums of K ranges where a call has few tiles; often 0); its
  * contents need no initialisation.
@@ -455,7 +456,7 @@ int gated_mm_backward(const void* dh, const void* x, int64_t ld_x, const void* W
  *          128 columns (I a multiple of 128), quantized from the unrounded
  *          float32 values by the rule of quant_8bit (eps 1e-10, range
  *          [-448, 448]): A and As of the next blockwise_scaled_mm. NULL, NULL
- *          when h is given.
+ *          when h is given. No output may overlap an input or another output.
  * workspace: blockwise_scaled_gated_mm_workspace_size bytes for the current
  * device, 16-byte aligned (float32 sums of K ranges where a call has few tiles,
  * or of a quantized call of few rows; often 0); no initialisation.
@@ -480,7 +481,7 @@ int blockwise_scaled_gated_mm(const void* A, const float* As, const void* W, con
  * scaling  [L] float32, or NULL for 1
  * base     [M, N] of dtype, row stride ld_base, or NULL for zeros; may be out
  *          itself, with the same stride
- * out      [M, N] of dtype, row stride ld_out
+ * out      [M, N] of dtype, row stride ld_out; may overlap no other argument
  * x A^T is summed and scaled in float32 and enters the second product as two
  * 16-bit terms (16 bits of it at least for bf16, 22 for f16); out is rounded once.
  * A row's result does not depend on the other rows. K and ld_x multiples of 8;

@@ -769,7 +769,7 @@ def blockwise_scaled_gated_mm(mat_a: torch.Tensor, mat_b: torch.Tensor, scales_a
     the unrounded products — the next ``blockwise_scaled_mm``'s ``mat_a`` and
     ``scales_a``. ``delta`` [M, 2I] (bf16/f16; the type of a 16-bit ``out``) is
     added before the activation. K must be a multiple of 128, I of 16 (of 128
-    when the result is quantized).
+    when the result is quantized). No output may overlap an input or another output.
     """
     act = _act(activation)
     quant = out_dtype == torch.float8_e4m3fn
@@ -830,7 +830,7 @@ def lora_mm(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, adapter
     same type (R a multiple of 8 up to 128; pad smaller ranks with zeros),
     ``adapter_ids`` [M] int32 (outside [0, L): no adapter), ``scaling`` [L]
     float32. ``base`` [M, N] is the shared projection's output (zeros when
-    None); ``out`` may be ``base`` itself. ``x``, ``base`` and ``out`` may have
+    None); ``out`` may be ``base`` itself and overlap nothing else. ``x``, ``base`` and ``out`` may have
     row strides, so a part of a merged projection's columns can be passed.
     Rows need no order, but rows of one request next to each other share the
     reads of its adapter. K must be a multiple of 8.
