@@ -5,7 +5,7 @@ GPU and laid out as the C ABI expects (``include/q8gemm.h``), then passes raw
 pointers, sizes and the current HIP stream to the library. Every step of the
 computation runs in the library's HIP kernels; there is no fallback, and
 importing this package fails loudly when ``libq8gemm.so`` is missing (build it
-with ``python -m int8_quantized_gemm_amd.build``).
+with ``python int8_quantized_gemm_amd/build.py``).
 
 Names and argument orders follow the pages' wrappers: sgl-kernel's
 ``sgl_per_token_group_quant_8bit``, ``fp8_blockwise_scaled_mm``,
@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "libq8gemm.so")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
-        f"{LIB_PATH} is missing: build it with `python -m int8_quantized_gemm_amd.build` "
+        f"{LIB_PATH} is missing: build it with `python int8_quantized_gemm_amd/build.py` "
         "(there is no CPU fallback)")
 
 _lib = ctypes.CDLL(LIB_PATH)

@@ -65,3 +65,14 @@ def test_sizes_are_asked_for_on_the_tensors_device(q8, monkeypatch):
     monkeypatch.setattr(q8, "_ws_sizes", {})
     assert [q8._scratch_size(d, sizes, 3, 4) for d in (0, 1, 0, 1)] == [107, 207, 107, 207]
     assert asked == [0, 1] and now == [0]
+
+
+def test_a_missing_library_names_a_command_that_builds_it(tmp_path):
+    """The package cannot be imported before it is built, so not `python -m` of it."""
+    pkg = tmp_path / "int8_quantized_gemm_amd"
+    pkg.mkdir()
+    (pkg / "__init__.py").write_text(open(os.path.join(ROOT, "int8_quantized_gemm_amd", "__init__.py")).read())
+    r = subprocess.run([sys.executable, "-c", "import int8_quantized_gemm_amd"], cwd=tmp_path, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode and "ImportError" in r.stderr and "`python int8_quantized_gemm_amd/build.py`" in r.stderr
+    assert os.path.exists(os.path.join(ROOT, "int8_quantized_gemm_amd", "build.py"))
